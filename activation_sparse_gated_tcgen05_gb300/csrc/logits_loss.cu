@@ -221,15 +221,18 @@ TW_DEV uint64_t sum_exp(const uint4& v, float m, const ExpK& k, uint64_t acc) {
 }
 
 // q exp(scale (x - m)) as 2^(k x + b) q2, one FMA for the exponent: b = fl(-k m),
-// and what that rounding leaves out of k m goes into q2.  (Where k m overflows,
-// -- logits at the type's limit -- the difference is taken first: `far`.)
+// and what that rounding leaves out of k m goes into q2, as 2^-rest = 1 - rest ln 2:
+// good to 6e-8 while |k m| < 2^14, where |rest| <= 2^-11.  From there on (logits
+// with a large offset, rows of nothing but a mask value, large scales) the
+// difference is taken first: `far`.
+constexpr float kNearExponent = 16384.0f;
 struct Scaled {
   float k, b, q, m;
   bool far;
 };
 TW_DEV Scaled make_scaled(const ExpK& k, float m, float q) {
   const float mk = __fmul_rn(m, k.hi);
-  if (!(fabsf(mk) < 1e38f)) return Scaled{k.hi, 0.0f, q, m, true};
+  if (!(fabsf(mk) < kNearExponent)) return Scaled{k.hi, 0.0f, q, m, true};
   const float rest = fmaf(m, k.hi, -mk);
   return Scaled{k.hi, -mk, q * fmaf(rest, -0.69314718f, 1.0f), m, false};
 }

@@ -368,13 +368,15 @@ TW_DEV PolicyRow load_policy(const Policy& P, int t) {
 }
 // Loss term of one token and its derivative by logp.  `over` and `under`: the
 // ratio is past the clip on the side where min() takes the clipped, constant branch.
+// Without an advantage r A is 0, also where r overflows (a NaN stays one).
 TW_DEV void policy_terms(const Policy& P, const PolicyRow& x, float logp, float& tok, float& coef) {
   tok = coef = 0.0f;
   if (x.w == 0.0f) return;
   const float r = P.old_logp ? expf(logp - x.old_logp) : 1.0f;
   const bool over = x.A > 0.0f && r > P.hi, under = x.A < 0.0f && r < P.lo;
-  tok = over ? -P.hi * x.A : under ? -P.lo * x.A : -r * x.A;
-  coef = over || under ? 0.0f : -r * x.A;
+  const float rA = x.A == 0.0f && r == INFINITY ? 0.0f : r * x.A;
+  tok = over ? -P.hi * x.A : under ? -P.lo * x.A : -rA;
+  coef = over || under ? 0.0f : -rA;
   if (P.kl != 0.0f) {
     const float q = x.ref_logp - logp;
     const float e = expm1f(q);  // exp(q) - 1 - q without the cancellation of exp(q) - 1

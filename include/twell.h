@@ -340,7 +340,7 @@ twell_status twell_token_logp(const twell_logits* logits, float* logp, float* ls
 /* The clipped policy loss with a KL term (Schulman et al. 2017, "Proximal
  * policy optimization algorithms"; the KL estimate is the one of Schulman
  * 2020, "Approximating KL divergence", k3).  All fp32 [rows]:
- *   advantage  A
+ *   advantage  A; 0 leaves the clipped term out, also where r overflows
  *   weight     w: the token's weight in the loss (a mask over the number of
  *              tokens, say); NULL = 1.  A weight of 0 leaves the token out of
  *              the loss and the gradient whatever the other terms are

@@ -1,0 +1,53 @@
+"""Losses at the limits of their formulas: what a term that does not count must not do to the ones that do."""
+import numpy as np
+import pytest
+import torch
+
+from activation_sparse_gated_tcgen05_gb300 import twell
+
+from step_reference import logits_reference, policy_reference
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(n):
+    return [torch.full((n,), float("nan"), device="cuda") for _ in range(4)]
+
+
+def logits(T, V, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(T, V, generator=g, device="cuda")
+    return x, torch.randint(0, V, (T,), generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("T,V", [(8, 40), (8, 9000), (160, 50001)])
+def test_no_advantage_under_a_ratio_past_the_type(T, V):
+    """exp(logp - old) overflows fp32, the advantage is 0: the term and its gradient are 0, the KL term's stay.
+    In 64 bits the ratio is finite."""
+    x, y = logits(T, V)
+    _, lp, _, live = logits_reference(x.double().cpu().numpy(), y.cpu().numpy())
+    old, ref, adv = lp - 0.05, lp + 0.1, np.ones(T)
+    old[::2] -= 100.0
+    adv[::2] = 0.0
+    dev = [torch.tensor(a, dtype=torch.float32, device="cuda") for a in (adv, old, ref)]
+    want, c = policy_reference(lp, live, adv, None, old, ref, kl=0.1)
+    for grad in (torch.empty_like(x), None):
+        tok, logp, lse, coef = rows(T)
+        loss = torch.zeros((), device="cuda")
+        twell.twell_policy_loss(twell.TwellLogits(x, y), twell.TwellPolicy(dev[0], None, dev[1], dev[2], kl_coeff=0.1), loss,
+                                tok, logp, lse, coef, dlogits=grad)
+        # |A| r and the KL term's parts are at most 1.3, each off by a log-probability's 5e-6 + 1e-6 |value|
+        assert np.all(np.abs(tok.double().cpu().numpy() - want) <= 4e-5)
+        assert np.all(np.abs(coef.double().cpu().numpy() - c) <= 4e-5)
+        assert abs(float(loss) - want.sum()) <= 4e-5 * T
+        assert grad is None or bool(torch.isfinite(grad).all())
+
+
+def test_no_advantage_keeps_a_row_that_is_nan():
+    x, y = logits(4, 60)
+    x[1, 3] = float("nan")
+    tok, logp, lse, coef = rows(4)
+    zero = torch.zeros(4, device="cuda")
+    twell.twell_policy_loss(twell.TwellLogits(x, y), twell.TwellPolicy(zero, None, zero - 100.0), zero[:1].clone(), tok, logp,
+                            lse, coef)
+    assert torch.isnan(tok).tolist() == torch.isnan(coef).tolist() == [False, True, False, False]

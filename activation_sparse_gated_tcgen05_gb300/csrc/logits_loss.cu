@@ -967,7 +967,8 @@ __global__ void __launch_bounds__(kPairThreads)
     const float d = (float)(beta * (gain[0] - gain[1]));
     seq_gain[2 * p] = (float)gain[0];
     seq_gain[2 * p + 1] = (float)gain[1];
-    pair_loss[p] = (1.0f - smooth) * softplus(-d) + smooth * softplus(d);
+    // without smoothing its term is 0, also at an infinite margin
+    pair_loss[p] = (1.0f - smooth) * softplus(-d) + (smooth > 0.0f ? smooth * softplus(d) : 0.0f);
     // d pair_loss / d delta = -(1 - e) sigmoid(-delta) + e sigmoid(delta)
     const float s = smooth / (1.0f + expf(-d)) - (1.0f - smooth) / (1.0f + expf(d));
     slope_sh = s * (beta / (float)pairs);

@@ -51,3 +51,27 @@ def test_no_advantage_keeps_a_row_that_is_nan():
     twell.twell_policy_loss(twell.TwellLogits(x, y), twell.TwellPolicy(zero, None, zero - 100.0), zero[:1].clone(), tok, logp,
                             lse, coef)
     assert torch.isnan(tok).tolist() == torch.isnan(coef).tolist() == [False, True, False, False]
+
+
+def preference(x, y, start, **kw):
+    T, pairs = x.shape[0], start.numel() // 2
+    o = [torch.full((n,), float("nan"), device="cuda") for n in (1, pairs, 2 * pairs, T, T, T)]
+    twell.twell_preference_loss(twell.TwellLogits(x, y), twell.TwellPreference(start, **kw), *o)
+    return o
+
+
+def test_rejected_answer_without_probability():
+    """A rejected token of probability zero: the margin is infinite and the pair's loss 0, as
+    -log sigmoid(inf) is; with smoothing the loss is infinite."""
+    x, y = logits(8, 50)
+    x[3, y[3]] = float("-inf")
+    start = torch.tensor([0, 2, 4, 6, 8], device="cuda")
+    loss, pair, gain, logp, lse, coef = preference(x, y, start, beta=0.5)
+    other = preference(x[4:].contiguous(), y[4:].contiguous(), start[:3], beta=0.5)
+    assert float(gain[1]) == float("-inf") and float(pair[0]) == 0.0
+    assert torch.equal(pair[1:], other[1]) and abs(float(loss) - 0.5 * float(other[0])) <= 1e-6 * float(other[0])
+    assert bool((coef[:4] == 0).all()) and bool((coef[4:] != 0).all())
+    d = torch.full_like(x, float("nan"))
+    twell.twell_logp_bwd(twell.TwellLogits(x, y), lse, coef, d)
+    assert bool((d[:4] == 0).all()) and bool(torch.isfinite(d).all())
+    assert float(preference(x, y, start, beta=0.5, label_smoothing=0.1)[1][0]) == float("inf")

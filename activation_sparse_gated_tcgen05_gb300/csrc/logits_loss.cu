@@ -40,7 +40,8 @@ ExpK make_exp_k(double scale) {
   const double k = scale * 1.4426950408889634074;
   float hi = (float)k;
   if ((double)hi >= k) hi = nextafterf(hi, 0.0f);
-  return ExpK{hi, (float)(k - (double)hi)};
+  const float lo = (float)(k - (double)hi);
+  return ExpK{hi, lo > 0.0f ? lo : nextafterf(0.0f, 1.0f)};  // it underflows only below 2^-97
 }
 
 struct Rows {

@@ -75,3 +75,19 @@ def test_rejected_answer_without_probability():
     twell.twell_logp_bwd(twell.TwellLogits(x, y), lse, coef, d)
     assert bool((d[:4] == 0).all()) and bool(torch.isfinite(d).all())
     assert float(preference(x, y, start, beta=0.5, label_smoothing=0.1)[1][0]) == float("inf")
+
+
+@pytest.mark.parametrize("T,V", [(5, 300), (3, 9000), (3, 90000)])
+@pytest.mark.parametrize("scale", [1e-36, 1e-38])
+def test_masked_entries_at_the_smallest_scales(T, V, scale):
+    """softmax(scale x) is uniform over what is not masked; ln of the count is right to 1e-6 and logp to LP."""
+    x, y = logits(T, V)
+    x[:, 1::2] = float("-inf")
+    y = y - y % 2
+    tok, logp, lse, coef = rows(T)
+    twell.twell_token_logp(twell.TwellLogits(x, y, scale), logp, lse)
+    want = -np.log((V + 1) // 2)
+    assert np.all(np.abs(logp.double().cpu().numpy() - want) <= 5e-6 + 1e-6 * abs(want))
+    x[0] = float("-inf")
+    twell.twell_token_logp(twell.TwellLogits(x, y, scale), logp, lse)
+    assert bool(torch.isnan(logp[0])) and bool(torch.isfinite(logp[1:]).all())

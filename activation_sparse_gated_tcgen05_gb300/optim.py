@@ -122,10 +122,13 @@ class AdamW(torch.optim.Optimizer):
                 kinds.setdefault((p.dtype, grads[p].dtype), []).append(p)
             for j, (kind, members) in enumerate(kinds.items()):
                 tensors = self._list((i, kind), members, [grads[p] for p in members])
-                twell.twell_adamw_step(
-                    tensors, step=g["step"], lr=float(g["lr"]), beta1=g["betas"][0],
-                    beta2=g["betas"][1], eps=g["eps"], weight_decay=g["weight_decay"],
-                    seed=self.seed + 64 * i + j, grad_scale=factor)
+                try:
+                    twell.twell_adamw_step(
+                        tensors, step=g["step"], lr=float(g["lr"]), beta1=g["betas"][0],
+                        beta2=g["betas"][1], eps=g["eps"], weight_decay=g["weight_decay"],
+                        seed=self.seed + 64 * i + j, grad_scale=factor)
+                finally:
+                    tensors.drop_grads()  # the list is kept, what zero_grad() frees is not
         return loss
 
     def load_state_dict(self, state_dict):

@@ -558,10 +558,14 @@ class TwellParams:
         """The gradients of the next steps, one for each parameter."""
         if len(grads) != self.count:
             raise ValueError("grads must have %d entries" % self.count)
-        self.grad_dtype = self._dtype("grads", grads)
+        dtype = self._dtype("grads", grads)
         for e, g in zip(self.c, grads):
             e.grad = None if g is None else _vec(g, e.n, "grad", g.dtype)
-        self.tensors[2] = list(grads)
+        self.tensors[2], self.grad_dtype = list(grads), dtype
+
+    def drop_grads(self):
+        """Lets go of the gradients; set_grads gives the next ones."""
+        self.tensors[2], self.grad_dtype = [None] * self.count, None
 
 
 class TwellGrads:
@@ -577,6 +581,11 @@ class TwellGrads:
             e.grad = _vec(g, g.numel(), "grad", g.dtype)
 
 
+def _has_grads(params):
+    if params.grad_dtype is None:
+        raise ValueError("the list's gradients were dropped: set_grads gives new ones")
+
+
 def twell_grad_norm_workspace_bytes() -> int:
     return int(load().twell_grad_norm_workspace_bytes())
 
@@ -584,6 +593,7 @@ def twell_grad_norm_workspace_bytes() -> int:
 def twell_grad_norm(params, max_norm: float, out, ws, stream=None):
     """out (fp32 [2]) = the global norm of the gradients of a TwellParams or TwellGrads, and
     min(1, max_norm / norm)."""
+    _has_grads(params)
     _check("twell_grad_norm", load().twell_grad_norm(
         params.c, params.count, params.grad_dtype, float(max_norm), _vec(out, 2, "out"), _ptr(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
@@ -594,6 +604,7 @@ def twell_adamw_step(params: TwellParams, step: int, lr: float = 1e-3, beta1: fl
                      seed: int = 0, grad_scale=None, stream=None):
     """One AdamW step; step counts from 1, grad_scale (fp32 [1] on the GPU) multiplies the
     gradients, seed and step choose the random numbers of 8-bit states."""
+    _has_grads(params)
     h = AdamW(lr, beta1, beta2, eps, weight_decay, int(step), int(seed) & 0xFFFFFFFFFFFFFFFF,
               _vec(grad_scale, 1, "grad_scale"), params.param_dtype, params.grad_dtype,
               params.state_bits)

@@ -129,6 +129,9 @@ class AdamW(torch.optim.Optimizer):
                         seed=self.seed + 64 * i + j, grad_scale=factor)
                 finally:
                     tensors.drop_grads()  # the list is kept, what zero_grad() frees is not
+                # the kernels' writes, for what autograd saved before them
+                torch.autograd.graph.increment_version(
+                    members + [self._copies[p] for p in members if p in self._copies])
         return loss
 
     def load_state_dict(self, state_dict):

@@ -65,3 +65,18 @@ def test_dropped_gradients_are_not_used_again(monkeypatch):
             call()
     L.set_grads([g])
     assert L.tensors[2] == [g] and L.grad_dtype == 1
+
+
+@pytest.mark.parametrize("copies", [False, True])
+def test_autograd_sees_what_a_step_wrote(calls, copies):
+    """A backward of a forward from before the step raises, as after the steps of PyTorch's optimizers."""
+    p, q, idle = parameters(6, 4, 2)
+    opt = AdamW([p, q, idle], bf16_copies=copies)
+    give_grads((p, q))
+    values = [t for t in (p, q) for t in ((t, opt.copy_of(t)) if copies else (t,))]
+    before, other = [t._version for t in values], idle._version
+    loss = (p * p).sum()
+    opt.step()
+    assert all(t._version > v for t, v in zip(values, before)) and idle._version == other
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()

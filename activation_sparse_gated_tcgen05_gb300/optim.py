@@ -25,9 +25,9 @@ class AdamW(torch.optim.Optimizer):
                  holds the last norm and the factor it led to
     bf16_copies  keeps a bf16 copy of every fp32 parameter, see copy_of()
 
-    lr, betas, eps, weight_decay may differ between groups.  Steps are counted by group, for all
-    of its parameters and whether or not the norm was finite.  step() launches on the current
-    stream and reads nothing back."""
+    lr, betas, eps, weight_decay may differ between groups.  Steps are counted for each
+    parameter from its first gradient on (state[p]["step"]), and whether or not the norm was
+    finite.  step() launches on the current stream and reads nothing back."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, state_bits: int = 32, max_norm: float = None,
@@ -44,7 +44,7 @@ class AdamW(torch.optim.Optimizer):
         self._keep_copies, self._copies, self._lists = bf16_copies, {}, {}
         self.last_norm, self._ws = None, None
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
-                                      weight_decay=weight_decay, step=0))
+                                      weight_decay=weight_decay))
 
     def add_param_group(self, group):
         super().add_param_group(group)
@@ -69,7 +69,7 @@ class AdamW(torch.optim.Optimizer):
     def _state(self, p):
         st = self.state[p]
         if "m" not in st:
-            st.update(twell.alloc_adamw_state(p, self.state_bits))
+            st.update(twell.alloc_adamw_state(p, self.state_bits), step=0)
         return st
 
     def _list(self, key, params, grads):
@@ -115,41 +115,45 @@ class AdamW(torch.optim.Optimizer):
                                   self.last_norm, self._ws)
             factor = self.last_norm[1:]
         for i, (g, ps) in enumerate(zip(self.param_groups, live)):
-            g["step"] += 1
-            # one list for each pair of types within the group
+            # one list for each pair of types and each step within the group
             kinds = {}
             for p in ps:
-                kinds.setdefault((p.dtype, grads[p].dtype), []).append(p)
-            for j, (kind, members) in enumerate(kinds.items()):
-                tensors = self._list((i, kind), members, [grads[p] for p in members])
+                kinds.setdefault((p.dtype, grads[p].dtype, self._state(p)["step"]), []).append(p)
+            for j, ((_, _, done), members) in enumerate(kinds.items()):
+                tensors = self._list((i, j), members, [grads[p] for p in members])
                 try:
                     twell.twell_adamw_step(
-                        tensors, step=g["step"], lr=float(g["lr"]), beta1=g["betas"][0],
+                        tensors, step=done + 1, lr=float(g["lr"]), beta1=g["betas"][0],
                         beta2=g["betas"][1], eps=g["eps"], weight_decay=g["weight_decay"],
-                        seed=self.seed + 64 * i + j, grad_scale=factor)
+                        seed=self.seed + 64 * i + j % 64 + (j // 64 << 40), grad_scale=factor)
                 finally:
                     tensors.drop_grads()  # the list is kept, what zero_grad() frees is not
+                for p in members:
+                    self.state[p]["step"] = done + 1
                 # the kernels' writes, for what autograd saved before them
                 torch.autograd.graph.increment_version(
                     members + [self._copies[p] for p in members if p in self._copies])
         return loss
 
     def load_state_dict(self, state_dict):
-        """Restores groups and moments.  (PyTorch would cast the moments to the parameters' types.)"""
+        """Restores groups and moments.  (PyTorch would cast the moments to the parameters' types.)
+        Takes dictionaries that count steps by group as well."""
         saved = state_dict["state"]
-        super().load_state_dict({"state": {}, "param_groups": state_dict["param_groups"]})
-        ids = [k for g in state_dict["param_groups"] for k in g["params"]]
+        groups = [dict(g) for g in state_dict["param_groups"]]
+        by_group = [(k, s) for g, s in [(g, g.pop("step", 0)) for g in groups] for k in g["params"]]
+        super().load_state_dict({"state": {}, "param_groups": groups})
         params = [p for g in self.param_groups for p in g["params"]]
-        for k, p in zip(ids, params):
+        for (k, step), p in zip(by_group, params):
             if not saved.get(k):  # no step has reached this parameter yet
                 continue
             want = twell.alloc_adamw_state(p, self.state_bits)
-            got = saved[k]
+            got = dict(saved[k])
+            step = got.pop("step", step)
             if set(got) != set(want) or any(
                     got[n].shape != t.shape or got[n].dtype != t.dtype for n, t in want.items()):
                 raise ValueError("the saved moments are of another form (state_bits) or size")
             for n, t in want.items():
                 t.copy_(got[n])
-            self.state[p] = want
+            self.state[p] = dict(want, step=int(step))
         self._lists.clear()
         self.refresh_copies()

@@ -1,4 +1,5 @@
 """What optim.AdamW keeps and hands on, with the library's calls replaced by recorders (no GPU needed)."""
+import copy
 import weakref
 
 import pytest
@@ -80,3 +81,47 @@ def test_autograd_sees_what_a_step_wrote(calls, copies):
     assert all(t._version > v for t, v in zip(values, before)) and idle._version == other
     with pytest.raises(RuntimeError, match="inplace"):
         loss.backward()
+
+
+def test_steps_count_by_parameter(calls):
+    """A parameter's first gradient is its step 1, whatever the others have behind them."""
+    p, q, r = parameters(5, 7, 3)
+    opt = AdamW([dict(params=[p, q]), dict(params=[r])])
+    for live in ((p,), (p, r), (p, q, r), (q,), (p, q)):
+        opt.zero_grad()
+        give_grads(live)
+        opt.step()
+    steps = [(n, sorted(t.numel() for t in ps)) for n, ps, _ in calls]
+    assert steps == [(1, [5]), (2, [5]), (1, [3]), (3, [5]), (1, [7]), (2, [3]), (2, [7]), (4, [5]), (3, [7])]
+    # no two lists of a step share their random numbers
+    third = [(kw["seed"], n) for n, _, kw in calls[3:6]]
+    assert len(set(third)) == 3
+
+
+def test_counts_survive_a_state_dict(calls):
+    p, q = parameters(5, 7)
+    opt = AdamW([p, q], state_bits=8)
+    for live in ((p,), (p, q)):
+        opt.zero_grad()
+        give_grads(live)
+        opt.step()
+    other = AdamW(parameters(5, 7), state_bits=8)
+    other.load_state_dict(copy.deepcopy(opt.state_dict()))
+    calls.clear()
+    give_grads(other.param_groups[0]["params"])
+    other.step()
+    assert sorted((n, ps[0].numel()) for n, ps, _ in calls) == [(2, 7), (3, 5)]
+    assert set(other.state_dict()["state"][0]) == set(opt.state_dict()["state"][0])
+
+
+def test_a_state_dict_that_counts_by_group(calls):
+    """Groups that hold the step for all their parameters, as this class wrote them before."""
+    p, q = parameters(5, 7)
+    moments = {i: {k: torch.full((n,), 0.5) for k in ("m", "v")} for i, n in enumerate((5, 7))}
+    group = dict(lr=0.5, betas=(0.9, 0.99), eps=1e-8, weight_decay=0.0, step=41, params=[0, 1])
+    opt = AdamW([p, q])
+    opt.load_state_dict(dict(state=moments, param_groups=[group]))
+    give_grads((p, q))
+    opt.step()
+    assert [(n, len(ps), kw["lr"]) for n, ps, kw in calls] == [(42, 2, 0.5)]
+    assert float(opt.state[p]["m"][0]) == 0.5

@@ -48,7 +48,24 @@ struct Hyper {
   float eps;
   uint32_t key;
   const float* grad_scale;
+  int* skipped;
+  int count_skip;  // this launch adds a skipped step to the count
+  // of the corrections where steps were skipped
+  float step, lr, ln_beta1, ln_beta2;
 };
+
+// What follows from the step: lr / (1 - beta1^t) and 1 / sqrt(1 - beta2^t).  The
+// host has them for t = step; where steps were skipped they are made here,
+// 1 - beta^t = -expm1(t ln beta), right to a few units of fp32's last place for any t.
+// (COUNTED, in kernels of their own: as constants they cost the others no registers.)
+struct Corrections {
+  float size, inv_root;
+};
+TW_DEV Corrections corrections(const Hyper& H, int skipped) {
+  if (skipped == 0) return Corrections{H.size, H.inv_root};
+  const float t = fmaxf(H.step - (float)skipped, 1.0f);
+  return Corrections{H.lr / -expm1f(t * H.ln_beta1), 1.0f / sqrtf(-expm1f(t * H.ln_beta2))};
+}
 
 // The tensor that holds a chunk: the last one whose first chunk is not past it.
 template <class L_>
@@ -241,7 +258,8 @@ TW_DEV void store_block(const Entry& e, const Hyper& H, long long blk, int lane,
 // fused), so the sum is an FMA with a factor of 1 that only the host knows.
 constexpr int kWarps = 8;
 template <typename P, typename G, int BITS, bool WIDE, int U>
-TW_DEV void step_blocks(const Entry& e, const Hyper& H, float gs, long long blk0, int lane) {
+TW_DEV void step_blocks(const Entry& e, const Hyper& H, const Corrections& C, float gs, long long blk0,
+                        int lane) {
   Quad g[U][2], p[U][2], m[U][2], r[U][2];
   uint32_t mc[U][2], vc[U][2];
   float ms[U], vs[U];
@@ -272,7 +290,7 @@ TW_DEV void step_blocks(const Entry& e, const Hyper& H, float gs, long long blk0
   }
   const uint64_t gs2 = f2_splat(gs), b1 = f2_splat(H.beta1), c1 = f2_splat(H.one_beta1);
   const uint64_t b2 = f2_splat(H.beta2), c2 = f2_splat(H.one_beta2), decay = f2_splat(H.decay);
-  const uint64_t one = f2_splat(H.one), size = f2_splat(-H.size), inv = f2_splat(H.inv_root), eps = f2_splat(H.eps);
+  const uint64_t one = f2_splat(H.one), size = f2_splat(-C.size), inv = f2_splat(C.inv_root), eps = f2_splat(H.eps);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const long long blk = blk0 + u * kWarps, i0 = blk * kBlock + 4 * lane;
@@ -343,21 +361,27 @@ TW_DEV void step_blocks(const Entry& e, const Hyper& H, float gs, long long blk0
 // and three 248 us, four and two 266 us).
 __host__ __device__ constexpr int blocks_of(int bits) { return bits == 32 ? 1 : 2; }
 
-template <typename P, typename G, int BITS, int MAX>
+template <typename P, typename G, int BITS, int MAX, bool COUNTED>
 __global__ void __launch_bounds__(32 * kWarps, BITS == 8 ? 4 : 5)
     adamw_kernel(const __grid_constant__ List<MAX> L, const Hyper H) {
   constexpr int U = blocks_of(BITS);
   const float gs = H.grad_scale ? *H.grad_scale : 1.0f;
-  if (!(fabsf(gs) <= 3.402823466e38f)) return;  // NaN or infinite: the step changes nothing
+  const int skipped = COUNTED ? *reinterpret_cast<volatile const int*>(H.skipped) : 0;
+  if (!(fabsf(gs) <= 3.402823466e38f)) {  // NaN or infinite: the step changes nothing
+    // (and no block uses the count that this one changes)
+    if (COUNTED && H.count_skip && blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(H.skipped, 1);
+    return;
+  }
+  const Corrections C = COUNTED ? corrections(H, skipped) : Corrections{H.size, H.inv_root};
   // last chunks first: those whose gradients the norm read last are still in L2
   const int chunk = (int)(gridDim.x - 1 - blockIdx.x);
   const Entry& e = L.e[find_entry(L, chunk)];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long blk0 = (long long)(chunk - e.chunk) * (U * kWarps) + warp;
   if (e.wide && (blk0 + (U - 1) * kWarps + 1) * kBlock <= e.n)
-    step_blocks<P, G, BITS, true, U>(e, H, gs, blk0, lane);
+    step_blocks<P, G, BITS, true, U>(e, H, C, gs, blk0, lane);
   else
-    step_blocks<P, G, BITS, false, U>(e, H, gs, blk0, lane);
+    step_blocks<P, G, BITS, false, U>(e, H, C, gs, blk0, lane);
 }
 
 // ------------------------------------------------------------------ norm
@@ -481,24 +505,24 @@ L_<MAX> shorter(const L_<kMaxTensors>& L) {
   return f;
 }
 
-template <typename P, typename G, int BITS>
+template <typename P, typename G, int BITS, bool COUNTED>
 void adamw_run(int grid, const List<kMaxTensors>& L, const Hyper& H, cudaStream_t s) {
   if (L.count <= kFewTensors)
-    adamw_kernel<P, G, BITS, kFewTensors>
+    adamw_kernel<P, G, BITS, kFewTensors, COUNTED>
         <<<grid, 32 * kWarps, 0, s>>>(shorter<List, kFewTensors>(L), H);
   else if (L.count <= kSomeTensors)
-    adamw_kernel<P, G, BITS, kSomeTensors>
+    adamw_kernel<P, G, BITS, kSomeTensors, COUNTED>
         <<<grid, 32 * kWarps, 0, s>>>(shorter<List, kSomeTensors>(L), H);
   else
-    adamw_kernel<P, G, BITS, kMaxTensors><<<grid, 32 * kWarps, 0, s>>>(L, H);
+    adamw_kernel<P, G, BITS, kMaxTensors, COUNTED><<<grid, 32 * kWarps, 0, s>>>(L, H);
 }
 
 template <typename P, typename G>
 void adamw_run(int bits, int grid, const List<kMaxTensors>& L, const Hyper& H, cudaStream_t s) {
   if (bits == 8)
-    adamw_run<P, G, 8>(grid, L, H, s);
+    H.skipped ? adamw_run<P, G, 8, true>(grid, L, H, s) : adamw_run<P, G, 8, false>(grid, L, H, s);
   else
-    adamw_run<P, G, 32>(grid, L, H, s);
+    H.skipped ? adamw_run<P, G, 32, true>(grid, L, H, s) : adamw_run<P, G, 32, false>(grid, L, H, s);
 }
 
 // Elements per thread block.
@@ -617,7 +641,7 @@ twell_status twell_adamw_step(const twell_param* params, int32_t count, const tw
     return TWELL_ERR_INVALID_ARG;
   twell_status st = check_list(params, count, a->grad_dtype);
   if (st != TWELL_OK) return st;
-  if (off(a->grad_scale, 4)) return TWELL_ERR_ALIGNMENT;
+  if (off(a->grad_scale, 4) || off(a->skipped, 4)) return TWELL_ERR_ALIGNMENT;
   for (int i = 0; i < count; ++i) {
     const twell_param& p = params[i];
     if (p.n == 0) continue;
@@ -639,6 +663,12 @@ twell_status twell_adamw_step(const twell_param* params, int32_t count, const tw
   H.eps = (float)a->eps;
   H.key = step_key(a->seed, a->step);
   H.grad_scale = a->grad_scale;
+  H.skipped = a->skipped;
+  H.count_skip = a->skipped != nullptr;
+  H.step = (float)a->step;
+  H.lr = (float)a->lr;
+  H.ln_beta1 = (float)log(a->beta1);  // -inf at 0: no correction
+  H.ln_beta2 = (float)log(a->beta2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   List<kMaxTensors> L;
   L.count = 0;
@@ -652,6 +682,7 @@ twell_status twell_adamw_step(const twell_param* params, int32_t count, const tw
       if (adamw_launch(a, (int)chunks, L, H, s) != cudaSuccess) return TWELL_ERR_CUDA;
       L.count = 0;
       chunks = 0;
+      H.count_skip = 0;
     }
     L.e[L.count++] = Entry{p.param, reinterpret_cast<uint16_t*>(p.copy), p.grad, p.m, p.v,
                            p.m_scale, p.v_scale, p.n, number, (int)chunks,

@@ -26,8 +26,9 @@ class AdamW(torch.optim.Optimizer):
     bf16_copies  keeps a bf16 copy of every fp32 parameter, see copy_of()
 
     lr, betas, eps, weight_decay may differ between groups.  Steps are counted for each
-    parameter from its first gradient on (state[p]["step"]), and whether or not the norm was
-    finite.  step() launches on the current stream and reads nothing back."""
+    parameter from its first gradient on (state[p]["step"]); those that changed nothing are
+    counted on the GPU (state[p]["skipped"]) and do not count for the bias corrections.  step()
+    launches on the current stream and reads nothing back."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, state_bits: int = 32, max_norm: float = None,
@@ -42,6 +43,7 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError("max_norm must be positive")
         self.state_bits, self.max_norm, self.seed = state_bits, max_norm, int(seed)
         self._keep_copies, self._copies, self._lists = bf16_copies, {}, {}
+        self._skips = {}  # each skipped count by its id: the tensor, how many parameters share it
         self.last_norm, self._ws = None, None
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
                                       weight_decay=weight_decay))
@@ -69,8 +71,25 @@ class AdamW(torch.optim.Optimizer):
     def _state(self, p):
         st = self.state[p]
         if "m" not in st:
-            st.update(twell.alloc_adamw_state(p, self.state_bits), step=0)
+            st.update(twell.alloc_adamw_state(p, self.state_bits), step=0, skipped=None)
         return st
+
+    def _skipped(self, members):
+        """The count of skipped steps that exactly these parameters share: each call raises it once.
+        Parameters that have so far stepped together with others leave with a copy of theirs."""
+        old = self.state[members[0]]["skipped"]
+        shared = self._skips.get(id(old))
+        if shared is not None and shared[1] == len(members):
+            return old
+        new = torch.zeros(1, dtype=torch.int32, device=members[0].device) if old is None else old.clone()
+        if shared is not None:
+            shared[1] -= len(members)
+            if shared[1] <= 0:
+                del self._skips[id(old)]
+        for p in members:
+            self.state[p]["skipped"] = new
+        self._skips[id(new)] = [new, len(members)]
+        return new
 
     def _list(self, key, params, grads):
         """The description of these parameters with their gradients; made again when a tensor
@@ -115,17 +134,19 @@ class AdamW(torch.optim.Optimizer):
                                   self.last_norm, self._ws)
             factor = self.last_norm[1:]
         for i, (g, ps) in enumerate(zip(self.param_groups, live)):
-            # one list for each pair of types and each step within the group
+            # one list for each pair of types and each count of steps within the group
             kinds = {}
             for p in ps:
-                kinds.setdefault((p.dtype, grads[p].dtype, self._state(p)["step"]), []).append(p)
-            for j, ((_, _, done), members) in enumerate(kinds.items()):
+                st = self._state(p)
+                kinds.setdefault((p.dtype, grads[p].dtype, st["step"], id(st["skipped"])), []).append(p)
+            for j, ((_, _, done, _), members) in enumerate(kinds.items()):
                 tensors = self._list((i, j), members, [grads[p] for p in members])
                 try:
                     twell.twell_adamw_step(
                         tensors, step=done + 1, lr=float(g["lr"]), beta1=g["betas"][0],
                         beta2=g["betas"][1], eps=g["eps"], weight_decay=g["weight_decay"],
-                        seed=self.seed + 64 * i + j % 64 + (j // 64 << 40), grad_scale=factor)
+                        seed=self.seed + 64 * i + j % 64 + (j // 64 << 40), grad_scale=factor,
+                        skipped=self._skipped(members))
                 finally:
                     tensors.drop_grads()  # the list is kept, what zero_grad() frees is not
                 for p in members:
@@ -140,20 +161,28 @@ class AdamW(torch.optim.Optimizer):
         Takes dictionaries that count steps by group as well."""
         saved = state_dict["state"]
         groups = [dict(g) for g in state_dict["param_groups"]]
-        by_group = [(k, s) for g, s in [(g, g.pop("step", 0)) for g in groups] for k in g["params"]]
+        by_group = [(i, k, step) for i, (g, step) in enumerate([(g, g.pop("step", 0)) for g in groups])
+                    for k in g["params"]]
         super().load_state_dict({"state": {}, "param_groups": groups})
         params = [p for g in self.param_groups for p in g["params"]]
-        for (k, step), p in zip(by_group, params):
+        counts = {}  # parameters with the same history share a count again
+        self._skips.clear()
+        for (i, k, step), p in zip(by_group, params):
             if not saved.get(k):  # no step has reached this parameter yet
                 continue
             want = twell.alloc_adamw_state(p, self.state_bits)
             got = dict(saved[k])
-            step = got.pop("step", step)
+            step, skipped = int(got.pop("step", step)), int(got.pop("skipped", 0))
             if set(got) != set(want) or any(
                     got[n].shape != t.shape or got[n].dtype != t.dtype for n, t in want.items()):
                 raise ValueError("the saved moments are of another form (state_bits) or size")
             for n, t in want.items():
                 t.copy_(got[n])
-            self.state[p] = dict(want, step=int(step))
+            key = (i, step, skipped)
+            if key not in counts:
+                counts[key] = torch.full((1,), skipped, dtype=torch.int32, device=p.device)
+                self._skips[id(counts[key])] = [counts[key], 0]
+            self._skips[id(counts[key])][1] += 1
+            self.state[p] = dict(want, step=step, skipped=counts[key])
         self._lists.clear()
         self.refresh_copies()

@@ -98,7 +98,8 @@ class AdamW(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
                 ("step", ctypes.c_int64), ("seed", ctypes.c_uint64),
                 ("grad_scale", ctypes.c_void_p), ("param_dtype", ctypes.c_int32),
-                ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32)]
+                ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("skipped", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -601,13 +602,14 @@ def twell_grad_norm(params, max_norm: float, out, ws, stream=None):
 
 def twell_adamw_step(params: TwellParams, step: int, lr: float = 1e-3, beta1: float = 0.9,
                      beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01,
-                     seed: int = 0, grad_scale=None, stream=None):
+                     seed: int = 0, grad_scale=None, stream=None, skipped=None):
     """One AdamW step; step counts from 1, grad_scale (fp32 [1] on the GPU) multiplies the
-    gradients, seed and step choose the random numbers of 8-bit states."""
+    gradients, seed and step choose the random numbers of 8-bit states, skipped (int32 [1] on the
+    GPU) counts the steps that changed nothing, for the bias corrections."""
     _has_grads(params)
     h = AdamW(lr, beta1, beta2, eps, weight_decay, int(step), int(seed) & 0xFFFFFFFFFFFFFFFF,
               _vec(grad_scale, 1, "grad_scale"), params.param_dtype, params.grad_dtype,
-              params.state_bits)
+              params.state_bits, _vec(skipped, 1, "skipped", torch.int32))
     _check("twell_adamw_step", load().twell_adamw_step(params.c, params.count, ctypes.byref(h),
                                                        _stream(stream)))
 

@@ -456,6 +456,10 @@ twell_status twell_grad_norm(const twell_param* params, int32_t count, int32_t g
  * as zero.  Results depend on nothing else and are bit-reproducible.
  *   grad_scale  device fp32 [1], e.g. out + 1 of twell_grad_norm; NULL = 1.
  *               NaN or infinite: the step changes nothing
+ *   skipped     device i32 [1], NULL = none: how many of the steps that `step`
+ *               counts changed nothing.  A call that changes nothing adds 1 (once, if
+ *               its list has any elements); others take their bias
+ *               corrections from step - *skipped (1 at least) in place of step
  * step >= 1; lr, weight_decay, eps >= 0; beta1, beta2 in [0, 1).  bf16
  * parameters without a master are rounded to nearest at each step.  A captured
  * graph replays the captured step's lr and step.  Tensors must not overlap. */
@@ -466,6 +470,7 @@ typedef struct twell_adamw {
   const float* grad_scale;
   int32_t param_dtype, grad_dtype; /* TWELL_BF16 / TWELL_F32, of every tensor of the list */
   int32_t state_bits;              /* 32 or 8 */
+  int32_t* skipped;
 } twell_adamw;
 twell_status twell_adamw_step(const twell_param* params, int32_t count, const twell_adamw* hyper,
                               void* stream);

@@ -1,5 +1,6 @@
 """What optim.AdamW keeps and hands on, with the library's calls replaced by recorders (no GPU needed)."""
 import copy
+import ctypes
 import weakref
 
 import pytest
@@ -125,3 +126,42 @@ def test_a_state_dict_that_counts_by_group(calls):
     opt.step()
     assert [(n, len(ps), kw["lr"]) for n, ps, kw in calls] == [(42, 2, 0.5)]
     assert float(opt.state[p]["m"][0]) == 0.5
+
+
+def test_skipped_counts_are_shared_by_those_that_step_together(calls):
+    """One count for each list: parameters that part take their own copy along, none is raised twice a step."""
+    p, q, h = torch.ones(5, requires_grad=True), torch.ones(7, requires_grad=True), torch.ones(3).bfloat16().requires_grad_()
+    opt = AdamW([p, q, h])
+
+    def step(*live):
+        calls.clear()
+        opt.zero_grad()
+        give_grads(live)
+        opt.step()
+        for _, ps, kw in calls:  # a skipped step, as the kernel counts it
+            kw["skipped"].add_(1)
+        return [kw["skipped"] for _, _, kw in calls]
+
+    def counts():
+        return [int(opt.state[t]["skipped"]) for t in (p, q, h)]
+
+    one, two = step(p, q, h)
+    assert one is not two and counts() == [1, 1, 1]
+    assert [x is y for x, y in zip(step(p, q, h), (one, two))] == [True, True]
+    alone, = step(p)
+    assert alone is not one and counts() == [3, 2, 2]
+    assert len({id(x) for x in step(p, q, h)}) == 3 and counts() == [4, 3, 3]
+    other = AdamW([torch.ones(n, requires_grad=True) for n in (5, 7)] + [torch.ones(3).bfloat16().requires_grad_()])
+    other.load_state_dict(copy.deepcopy(opt.state_dict()))
+    calls.clear()
+    give_grads(other.param_groups[0]["params"])
+    other.step()
+    assert sorted(int(kw["skipped"]) for _, _, kw in calls) == [3, 3, 4]
+    assert len({kw["skipped"].data_ptr() for _, _, kw in calls}) == 3
+
+
+def test_skipped_count_is_checked():
+    lib = twell.load()
+    args = (1e-3, 0.9, 0.999, 1e-8, 0.0, 1, 0, None, 1, 1, 32)
+    assert lib.twell_adamw_step(None, 0, ctypes.byref(twell.AdamW(*args, 18)), None) == 3
+    assert lib.twell_adamw_step(None, 0, ctypes.byref(twell.AdamW(*args, 16)), None) == 0

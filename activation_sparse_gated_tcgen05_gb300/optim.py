@@ -48,6 +48,20 @@ class AdamW(torch.optim.Optimizer):
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
                                       weight_decay=weight_decay))
 
+    def __getstate__(self):
+        """For copy and pickle: PyTorch's part and the options, the copies and the last norm; what
+        describes or shares tensors is made anew."""
+        keep = ("state_bits", "max_norm", "seed", "_keep_copies", "_copies", "last_norm")
+        return dict(super().__getstate__(), **{k: getattr(self, k) for k in keep})
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._lists, self._skips, self._ws = {}, {}, None
+        for st in self.state.values():
+            count = st.get("skipped")
+            if count is not None:
+                self._skips.setdefault(id(count), [count, 0])[1] += 1
+
     def add_param_group(self, group):
         super().add_param_group(group)
         for p in self.param_groups[-1]["params"]:
@@ -128,6 +142,7 @@ class AdamW(torch.optim.Optimizer):
             dev = next(iter(grads)).device
             if self.last_norm is None:
                 self.last_norm = torch.zeros(2, dtype=torch.float32, device=dev)
+            if self._ws is None:
                 self._ws = torch.empty(twell.twell_grad_norm_workspace_bytes(), dtype=torch.uint8,
                                        device=dev)
             twell.twell_grad_norm(twell.TwellGrads(list(grads.values())), self.max_norm,

@@ -158,3 +158,16 @@ def test_skipped_count_of_a_call(bits):
     twell.twell_adamw_step(B, 3, grad_scale=torch.full((1,), float("nan"), device="cuda"))  # without a count
     with pytest.raises(ValueError, match="skipped"):
         twell.twell_adamw_step(B, 3, skipped=torch.zeros(1, device="cuda"))
+
+
+def test_deepcopy_steps_on():
+    p = randn(500).requires_grad_()
+    opt = AdamW([p], bf16_copies=True, state_bits=8, max_norm=1.0, seed=2)
+    p.grad = randn(500, seed=1)
+    opt.step()
+    other = copy.deepcopy(opt)
+    (q,) = other.param_groups[0]["params"]
+    q.grad = p.grad.clone()
+    opt.step()
+    other.step()
+    assert torch.equal(p, q) and torch.equal(opt.copy_of(p), other.copy_of(q)) and opt.copy_of(p) is not other.copy_of(q)

@@ -1,6 +1,7 @@
 """What optim.AdamW keeps and hands on, with the library's calls replaced by recorders (no GPU needed)."""
 import copy
 import ctypes
+import io
 import weakref
 
 import pytest
@@ -165,3 +166,30 @@ def test_skipped_count_is_checked():
     args = (1e-3, 0.9, 0.999, 1e-8, 0.0, 1, 0, None, 1, 1, 32)
     assert lib.twell_adamw_step(None, 0, ctypes.byref(twell.AdamW(*args, 18)), None) == 3
     assert lib.twell_adamw_step(None, 0, ctypes.byref(twell.AdamW(*args, 16)), None) == 0
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "pickle"])
+def test_copies_of_an_optimizer(calls, how):
+    """A copied or pickled optimizer has its options, its parameters' states and bf16 copies, and steps."""
+    p, q = parameters(5, 7)
+    opt = AdamW([p, q], lr=0.25, state_bits=8, max_norm=2.0, bf16_copies=True, seed=9)
+    give_grads((p,))
+    opt.step()
+    assert not opt.state[q]  # looked at, never stepped
+    if how == "deepcopy":
+        other = copy.deepcopy(opt)
+    else:
+        buf = io.BytesIO()
+        torch.save(opt, buf)
+        buf.seek(0)
+        other = torch.load(buf, weights_only=False)
+    assert (other.state_bits, other.max_norm, other.seed, other.param_groups[0]["lr"]) == (8, 2.0, 9, 0.25)
+    p2, q2 = other.param_groups[0]["params"]
+    assert p2 is not p and torch.equal(p2, p) and torch.equal(other.copy_of(p2), opt.copy_of(p))
+    assert other.copy_of(p2).data_ptr() != opt.copy_of(p).data_ptr()
+    calls.clear()
+    give_grads((p2, q2))
+    other.step()
+    assert sorted((n, t[0].data_ptr()) for n, t, _ in calls) == sorted([(2, p2.data_ptr()), (1, q2.data_ptr())])
+    # what the copy does not do to the original
+    assert "m" not in opt.state[q] and p.grad is not None

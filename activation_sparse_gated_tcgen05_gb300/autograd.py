@@ -17,7 +17,8 @@ them as `bf16`, and nothing is cast.
 ``token_logp``, ``policy_loss`` and ``preference_loss`` take logits [rows][vocab]
 (bf16 or fp32, rows contiguous) and return fp32 results; their backward is one
 kernel that reads the logits again, so they hold nothing of the logits' size
-between forward and backward.  A training loop that wants loss and gradient
+between forward and backward.  It has no derivative of its own: a second
+derivative raises.  A training loop that wants loss and gradient
 of the policy loss in one pass calls twell.twell_policy_loss with `dlogits`.
 """
 from __future__ import annotations
@@ -117,6 +118,24 @@ def _vector(t):
     return None if t is None else t.detach().to(torch.float32).contiguous()
 
 
+class _Once(torch.autograd.Function):
+    """A gradient that a kernel wrote, with what it depends on: its own derivative raises.  (PyTorch's
+    once_differentiable looks at the incoming gradient alone, not at the logits.)"""
+
+    @staticmethod
+    def forward(ctx, d, *of):
+        return d
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the losses over logits are once_differentiable: their gradients are a "
+                           "kernel's and have no derivative")
+
+
+def _once(d, *of):
+    return _Once.apply(d, *of) if torch.is_grad_enabled() else d
+
+
 class _TokenLogp(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, target, scale: float):
@@ -133,7 +152,7 @@ class _TokenLogp(torch.autograd.Function):
         d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         twell.twell_logp_bwd(twell.TwellLogits(logits.detach(), target, ctx.scale), lse,
                              _vector(dlogp), d)
-        return d, None, None
+        return _once(d, logits, dlogp), None, None
 
 
 def token_logp(logits, target, scale: float = 1.0):
@@ -163,7 +182,7 @@ class _CoefLoss(torch.autograd.Function):
         d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         twell.twell_logp_bwd(twell.TwellLogits(logits.detach(), target, ctx.scale), lse, coef, d,
                              dloss=_vector(dloss))
-        return d, None, None, None
+        return _once(d, logits, dloss), None, None, None
 
 
 def policy_loss(logits, target, advantage, weight=None, old_logp=None, ref_logp=None,

@@ -49,7 +49,7 @@ class SparseGatedFFNFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, wgT, wuT, wd, l1_coeff: float, tile_n: int, tile_cap: int,
-                route_fraction: float, stats: Optional[dict], bf16):
+                route_fraction: float, stats: Optional[dict], bf16=None):
         if x.dim() != 2:
             raise ValueError("x must be [tokens][d_model]")
         if bf16 is not None and not (len(bf16) == 3 and all(

@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from activation_sparse_gated_tcgen05_gb300.autograd import policy_loss, preference_loss, token_logp
+from activation_sparse_gated_tcgen05_gb300.autograd import (SparseGatedFFNFunction, policy_loss, preference_loss,
+                                                            sparse_gated_ffn, token_logp)
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,16 @@ def test_second_derivatives_are_refused(which):
     d, = torch.autograd.grad(loss() * up, x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         torch.autograd.grad(d.sum(), up)
+
+
+def test_ffn_function_without_copies():
+    """The class itself with the nine arguments it had before it took bf16 copies."""
+    x, ws = randn(64, 256).bfloat16(), [(randn(1024, 256, seed=k) * 0.06).requires_grad_() for k in (1, 2, 3)]
+    y = SparseGatedFFNFunction.apply(x, *ws, 2e-5, 64, 16, 0.03, None)
+    y.float().sum().backward()
+    got = [w.grad for w in ws]
+    for w in ws:
+        w.grad = None
+    z = sparse_gated_ffn(x, *ws, tile_n=64, tile_cap=16)
+    z.float().sum().backward()
+    assert torch.equal(y, z) and all(torch.equal(a, w.grad) for a, w in zip(got, ws))

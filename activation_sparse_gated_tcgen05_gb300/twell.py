@@ -176,8 +176,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> int:
     if stream is None:
-        # the raw handle: a Stream object would cost more than most of these calls
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the raw handle: a Stream object would cost more than most of these calls; PyTorch does not
+        # promise the call that gives it, so the object is there for one without
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -171,3 +171,15 @@ def test_deepcopy_steps_on():
     opt.step()
     other.step()
     assert torch.equal(p, q) and torch.equal(opt.copy_of(p), other.copy_of(q)) and opt.copy_of(p) is not other.copy_of(q)
+
+
+def test_a_gradient_laid_out_another_way():
+    """A transposed gradient's elements meet their own parameters.  The first step moves each by lr against its
+    gradient's sign; none is 0."""
+    w = randn(8, 16).requires_grad_()
+    opt = AdamW([w], lr=0.1, weight_decay=0.0)
+    w.grad = (torch.arange(128.0, device="cuda").view(16, 8) - 60.5).t()
+    before = w.detach().clone()
+    opt.step()
+    # lr g / (|g| + eps): 0.1 to a few 2^-24 of the parameter
+    assert torch.allclose(before - w.detach(), 0.1 * torch.sign(w.grad), rtol=0.0, atol=2e-6)

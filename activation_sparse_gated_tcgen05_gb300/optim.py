@@ -88,29 +88,31 @@ class AdamW(torch.optim.Optimizer):
             st.update(twell.alloc_adamw_state(p, self.state_bits), step=0, skipped=None)
         return st
 
-    def _skipped(self, members):
-        """The count of skipped steps that exactly these parameters share: each call raises it once.
-        Parameters that have so far stepped together with others leave with a copy of theirs."""
-        old = self.state[members[0]]["skipped"]
+    def _skipped(self, states):
+        """The count of skipped steps that exactly the parameters of these states share: each call
+        raises it once.  Parameters that have so far stepped together with others leave with a copy
+        of theirs."""
+        old = states[0]["skipped"]
         shared = self._skips.get(id(old))
-        if shared is not None and shared[1] == len(members):
+        if shared is not None and shared[1] == len(states):
             return old
-        new = torch.zeros(1, dtype=torch.int32, device=members[0].device) if old is None else old.clone()
+        if old is None:
+            new = torch.zeros(1, dtype=torch.int32, device=states[0]["m"].device)
+        else:
+            new = old.clone()
         if shared is not None:
-            shared[1] -= len(members)
+            shared[1] -= len(states)
             if shared[1] <= 0:
                 del self._skips[id(old)]
-        for p in members:
-            self.state[p]["skipped"] = new
-        self._skips[id(new)] = [new, len(members)]
+        for st in states:
+            st["skipped"] = new
+        self._skips[id(new)] = [new, len(states)]
         return new
 
-    def _list(self, key, params, grads):
+    def _list(self, key, params, grads, states, copies):
         """The description of these parameters with their gradients; made again when a tensor
         has moved."""
-        states = [self._state(p) for p in params]
         names = ("m", "v") + (("m_scale", "v_scale") if self.state_bits == 8 else ())
-        copies = [self._copies.get(p) for p in params]
         where = [p.data_ptr() for p in params] + [s[n].data_ptr() for s in states for n in names]
         where += [0 if c is None else c.data_ptr() for c in copies]
         if key not in self._lists or self._lists[key][0] != where:
@@ -130,45 +132,49 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        live = [[p for p in g["params"] if p.grad is not None] for g in self.param_groups]
-        grads = {p: p.grad if p.grad.is_contiguous() else p.grad.contiguous()
-                 for ps in live for p in ps}
+        # (parameter, gradient) by group
+        live = [[(p, g if g.is_contiguous() else g.contiguous())
+                 for p, g in [(p, p.grad) for p in group["params"]] if g is not None]
+                for group in self.param_groups]
+        grads = [g for pairs in live for _, g in pairs]
         if not grads:
             return loss
         factor = None
         if self.max_norm is not None:
-            if len({g.dtype for g in grads.values()}) > 1:
+            if len({g.dtype for g in grads}) > 1:
                 raise ValueError("max_norm needs gradients of one type")
-            dev = next(iter(grads)).device
+            dev = grads[0].device
             if self.last_norm is None:
                 self.last_norm = torch.zeros(2, dtype=torch.float32, device=dev)
             if self._ws is None:
                 self._ws = torch.empty(twell.twell_grad_norm_workspace_bytes(), dtype=torch.uint8,
                                        device=dev)
-            twell.twell_grad_norm(twell.TwellGrads(list(grads.values())), self.max_norm,
+            twell.twell_grad_norm(twell.TwellGrads(grads), self.max_norm,
                                   self.last_norm, self._ws)
             factor = self.last_norm[1:]
-        for i, (g, ps) in enumerate(zip(self.param_groups, live)):
+        for i, (group, pairs) in enumerate(zip(self.param_groups, live)):
             # one list for each pair of types and each count of steps within the group
             kinds = {}
-            for p in ps:
+            for p, g in pairs:
                 st = self._state(p)
-                kinds.setdefault((p.dtype, grads[p].dtype, st["step"], id(st["skipped"])), []).append(p)
-            for j, ((_, _, done, _), members) in enumerate(kinds.items()):
-                tensors = self._list((i, j), members, [grads[p] for p in members])
+                kinds.setdefault((p.dtype, g.dtype, st["step"], id(st["skipped"])), []).append((p, g, st))
+            for j, ((dtype, _, done, _), members) in enumerate(kinds.items()):
+                ps, gs, states = map(list, zip(*members))
+                copied = self._keep_copies and dtype == torch.float32
+                copies = [self._copies[p] for p in ps] if copied else [None] * len(ps)
+                tensors = self._list((i, j), ps, gs, states, copies)
                 try:
                     twell.twell_adamw_step(
-                        tensors, step=done + 1, lr=float(g["lr"]), beta1=g["betas"][0],
-                        beta2=g["betas"][1], eps=g["eps"], weight_decay=g["weight_decay"],
+                        tensors, step=done + 1, lr=float(group["lr"]), beta1=group["betas"][0],
+                        beta2=group["betas"][1], eps=group["eps"], weight_decay=group["weight_decay"],
                         seed=self.seed + 64 * i + j % 64 + (j // 64 << 40), grad_scale=factor,
-                        skipped=self._skipped(members))
+                        skipped=self._skipped(states))
                 finally:
                     tensors.drop_grads()  # the list is kept, what zero_grad() frees is not
-                for p in members:
-                    self.state[p]["step"] = done + 1
+                for st in states:
+                    st["step"] = done + 1
                 # the kernels' writes, for what autograd saved before them
-                torch.autograd.graph.increment_version(
-                    members + [self._copies[p] for p in members if p in self._copies])
+                torch.autograd.graph.increment_version(ps + copies if copied else ps)
         return loss
 
     def load_state_dict(self, state_dict):

@@ -7,6 +7,9 @@
 //   logp = scale (x_y - X) - ln s,  softmax_v = exp(scale (x_v - X)) / s.
 // The difference is taken first, so neither a large offset of the logits nor
 // a mask of the type's lowest value loses or overflows anything.
+//
+// Times below are of whole calls in a row, by events, with no row ignored, inputs
+// that do not fit L2 or alternate, and the SMs at 2070 MHz.
 #include <math.h>
 
 #include "common.cuh"
@@ -419,7 +422,7 @@ TW_DEV MaxSum cluster_stats(const MaxSum& a, int CL, const ExpK& k) {
 }
 
 // Statistics, log-probability and loss term of each row, and with GRAD its
-// gradient.  Without GRAD it is bound by the reads (8192 x 65536 bf16 130 us,
+// gradient.  Without GRAD it is bound by the reads (8192 x 65536 bf16 150 us,
 // 105 % of the copy rate), with it by what the head of policy_ring_kernel says.
 // A row is taken by G threads of a block of NT, or (G = NT) by the
 // blocks of a cluster (gridDim.x = rows * cluster), a contiguous share of its
@@ -539,11 +542,11 @@ __global__ void __launch_bounds__(NT, MINB)
 // What bounds it: a row moves 2 (bf16) or 4 bytes an entry in and out, and
 // takes 13.7 warp instructions per 32 entries, of which the SM has 23 to spend
 // at the memory's rate.  A kernel with a block to a row (rows_kernel) leaves the
-// memory idle while blocks start, wait for their first loads and join their sums: 77 %
-// of the copy rate at 4096 x 131072 bf16, 17.8 instructions.  Here one producer
+// memory idle while blocks start, wait for their first loads and join their sums: 72 %
+// of the copy rate at 4096 x 131072 bf16 (442 us), 17.8 instructions.  Here one producer
 // warp copies the block's rows into a ring of kRing slots in shared memory
 // (cp.async.bulk), ahead of NCW consumer warps and across row boundaries:
-// 94 % there, 98 % at 8192 x 131072.  A slot takes kSlotPass chunks a
+// 94 % there (337 us), 98 % at 8192 x 131072 (646 us).  A slot takes kSlotPass chunks a
 // consumer thread: with two, and a check of every chunk's bounds, a kernel of
 // this form took 22.7 instructions and was slower than rows_kernel.
 // A row is read twice: for its statistics, then for its gradient.  Its last
@@ -1075,14 +1078,16 @@ twell_status launch_rows(const char* name, const Rows& R, const Policy& P, const
   const long long bytes = chunks * 16, sms = num_sms();
   auto groups = [&](int per_block) { return (unsigned)((R.rows + per_block - 1) / per_block); };
   // Few rows: as many blocks to each as fill the GPU, while each has a chunk
-  // for every thread; long rows up to three blocks to an SM (policy, bf16: 100 x 128000
-  // 14 us against 23 us; 100 x 32000 10 us with one to an SM, 11 us with two).
+  // for every thread; long rows up to three blocks to an SM.  (In a graph, one, two and
+  // three blocks: 100 x 128000 bf16 policy 27.5, 20.0 and 15.6 us, logp 11.8, 9.8 and 8.4;
+  // 100 x 32000 logp 5.0, 5.6 and 5.4, but policy 10.0, 9.2 and 8.4.)
   const long long places = (bytes > 128 * 1024 ? 3 : 1) * sms;
   int cl = 1;
   while (cl < 8 && R.rows * cl * 2 <= places && chunks > (long long)cl * 2 * 256) cl *= 2;
   // A warp to a row where rows are short, or many and not long: warps wait for
   // nobody but themselves.  (Against a block to a row, logp: 16384 x 4000 bf16
-  // 27 us to 72 us, 4000 x 16000 25 us to 34 us; policy: 64 us to 118 us, 59 us to 69 us.)
+  // 26 us to 76 us, 4000 x 16000 24 us to 32 us; policy: 62 us to 106 us, 57 us to 61 us;
+  // in a graph 311 x 2048 logp 2.7 to 3.2, policy 6.1 to 5.3.)
   const bool many = R.rows >= 16 * sms;
   if constexpr (GRAD) {
     if (bytes <= 4096 || (many && bytes <= 12288))
@@ -1096,8 +1101,12 @@ twell_status launch_rows(const char* name, const Rows& R, const Policy& P, const
       return launch_rows_as<E, MODE, GRAD, 32, 4, 256, 5>(R, P, o, d, dstride, groups(8), 1, s);
     if (many && bytes <= 65536)
       return launch_rows_as<E, MODE, GRAD, 32, 8, 256, 4>(R, P, o, d, dstride, groups(8), 1, s);
-    // two warps: 2047 x 50001 bf16 35 us, four 37 us, one 39 us, a block 43 us;
-    // four: 8192 x 65536 bf16 150 us, two and a block 160 us
+    // Times by one (of 8 chunks), two and four warps and a block to a row, bf16.  64 KiB: 2439
+    // rows 30, 32, 29 and 29 us, 9735 rows 94, 91, 90 and 93.  96 KiB: 1223 rows 32, 25, 26
+    // and 24, 2047 rows of 98 KiB 39, 35, 37 and 41, 2439 rows 41, 45, 41 and 40, 4871 rows 77,
+    // 74, 70 and 71.  128 KiB: 615 rows 34, 25, 18 and 19, 1223 rows 40, 31, 32 and 30, 8192
+    // rows 155, 159, 150 and 151.  160 KiB: 1223 rows 49, 37, 40 and 36, 8192 rows 197, 201, 189
+    // and 188.  256 KiB: 4096 rows 160, 155, 157 and 151.
     if (R.rows >= 8 * sms && bytes <= 112 * 1024)
       return launch_rows_as<E, MODE, GRAD, 64, 8, 256, 4>(R, P, o, d, dstride, groups(4), 1, s);
     if (R.rows >= 4 * sms && bytes <= 160 * 1024)
@@ -1128,11 +1137,15 @@ template <typename E>
 twell_status launch_policy_grad(const Rows& R, const Policy& P, const Outs& o, void* d,
                                 long long dstride, int* next, cudaStream_t s) {
   if (R.rows == 0) return TWELL_OK;
-  // Long rows, one at least for every block: the ring (4096 x 131072 bf16 337 us
-  // against 410 us by rows_kernel, 8192 x 65536 332 us against 394 us, 1536 x 100000 fp32
-  // 206 us against 277 us), one block of 16 warps to an SM, up to 160 KiB two of 8, up to
-  // 112 KiB four of 4 where each block gets some rows (8192 x 50001 278 us and 293 us, 8192 x
-  // 24000 146 us and 154 us; 4096 x 24000 83 us both; 2432 x 50000 97 us and 93 us).
+  // Long rows, one at least for every block: the ring, one block of 16 warps to an SM, up
+  // to 160 KiB two of 8, up to 112 KiB four of 4 where each block gets some rows.  Times by
+  // rows_kernel and by the rings of 4, 8 and 16 warps, bf16 but where it says fp32:
+  // 47 KiB, 4096 rows 82, 79, 84, 119 us, 8192 rows 152, 137, 153, 225; 98 KiB, 2047 rows 87,
+  // 90, 93, 109, 4096 rows 151, 148, 164, 201, 8192 rows 291, 268, 304, 388; 128 KiB, 1223 rows
+  // 73, 77, 68, 68, 8192 rows 377, 360, 330, 360; 176 KiB, 2439 rows 184, 180, 153, 164; 256 KiB,
+  // 1223 rows 159, 160, 123, 117, 8192 rows 877, 885, 694, 646; fp32 391 KiB, 1536 rows 286, 290,
+  // 254, 204.  With one to four rows to a block it does not gain yet: 117 KiB, 310 rows 25, 27,
+  // 34, 33, 620 rows 45, 52, 50, 49; 176 KiB, 160 rows 22, 29, 25, 30, 620 rows 65, 71, 64, 64.
   const long long bytes = chunks_of(R, sizeof(E)) * 16, sms = num_sms();
   if (bytes > 160 * 1024 && R.rows >= sms)
     return launch_ring_as<E, 16>(R, P, o, d, dstride, next, s);
